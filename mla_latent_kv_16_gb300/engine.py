@@ -66,15 +66,16 @@ class MLADecodeLayer:
         self.dev_error = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.num_splits = w.num_splits if num_splits is None else num_splits
         B, Lq = w.batch, w.q_len
-        self.splits = capi.mla_decode_num_splits(B, Lq, w.max_pages_per_seq, self.P, self.num_splits, self.H,
-                                                 self.cache_dtype)
-        need = capi.mla_decode_workspace_size(B, Lq, w.max_pages_per_seq, self.P, self.num_splits, self.H,
-                                              self.cache_dtype)
+        # (of the table's width, by which the calls choose their splits)
+        width = self.block_table.shape[1]
         if window > 0:
-            self.splits = capi.mla_decode_window_num_splits(B, Lq, self.block_table.shape[1], self.P, window, sinks,
-                                                            self.num_splits, self.H, self.cache_dtype)
-            need = capi.mla_decode_window_workspace_size(B, Lq, self.block_table.shape[1], self.P, window, sinks,
-                                                         self.num_splits, self.H, self.cache_dtype)
+            args = (B, Lq, width, self.P, window, sinks, self.num_splits, self.H, self.cache_dtype)
+            self.splits = capi.mla_decode_window_num_splits(*args)
+            need = capi.mla_decode_window_workspace_size(*args)
+        else:
+            args = (B, Lq, width, self.P, self.num_splits, self.H, self.cache_dtype)
+            self.splits = capi.mla_decode_num_splits(*args)
+            need = capi.mla_decode_workspace_size(*args)
         self.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
         self.q_lat = torch.empty(B, Lq, self.H, 512, dtype=self.act, device=self.device)
         self.u = torch.empty(B, Lq, self.H, 512, dtype=self.act, device=self.device)

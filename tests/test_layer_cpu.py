@@ -1,0 +1,45 @@
+"""What MLADecodeLayer sets up on the host: buffer sizes, refused arguments, the page state
+(no GPU needed: nothing is launched)."""
+import pytest
+import torch
+
+from mla_latent_kv_16_gb300 import build
+
+
+@pytest.fixture(scope="module")
+def capi():
+    build.build()
+    from mla_latent_kv_16_gb300 import capi as C
+    C.load()
+    return C
+
+
+def make(seqs, page, width, heads=128, cache="bf16", table=None, lens=None, pages_each=1, **kw):
+    from mla_latent_kv_16_gb300 import workloads as W
+    from mla_latent_kv_16_gb300.engine import MLADecodeLayer
+    act = "f32" if cache == "f32" else "bf16"
+    w = W.Workload("layer", seqs, 1, heads, [pages_each * page] * seqs, page, act, cache, 0)
+    weights = [torch.zeros(heads, 128, 512, dtype=W.TORCH_DTYPE[act]) for _ in range(2)]
+    if table is None:
+        table = torch.full((seqs, width), -1, dtype=torch.int32)
+    return MLADecodeLayer(w, *weights, table, torch.zeros(seqs, dtype=torch.int32) if lens is None else lens, device="cpu",
+                          **kw)
+
+
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("cache,heads,splits", [("bf16", 128, None), ("bf16", 128, 9), ("e4m3", 128, None), ("bf16", 16, None),
+                                                ("f32", 16, 7)])
+def test_workspace_is_sized_by_the_table(capi, cache, heads, splits, window):
+    """The calls take their split count from the table's width, which may exceed what the workload's
+    sequences need: the layer's count and workspace have to be those."""
+    layer = make(8, 64, 11, heads, cache, num_splits=splits, window=window, sinks=3 if window else 0)
+    asked = splits or 0
+    if window:
+        args = (8, 1, 11, 64, window, 3, asked, heads, cache)
+        want, need = capi.mla_decode_window_num_splits(*args), capi.mla_decode_window_workspace_size(*args)
+    else:
+        args = (8, 1, 11, 64, asked, heads, cache)
+        want, need = capi.mla_decode_num_splits(*args), capi.mla_decode_workspace_size(*args)
+    assert want > 1
+    assert layer.splits == want
+    assert layer.workspace.numel() >= need
