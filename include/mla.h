@@ -435,6 +435,10 @@ mla_status_t mla_prefill_window(const void *q_nope, const void *q_rope, const vo
  *     source's page is written or freed. Requests without such a page get -1, -1, 0.
  *   - New pages are the lowest-numbered free ones. A request that needs more
  *     than are left after the earlier requests is refused (MLA_DEVERR_NO_PAGE).
+ *   - A request that copies rows of the source's partly filled last page, or puts
+ *     new tokens behind them, is refused (MLA_DEVERR_BAD_PAGE) where the row holds
+ *     no page of the pool there. An entry of a shared page that lies outside the
+ *     pool is not shared: it becomes -1 in the fork and raises MLA_DEVERR_BAD_PAGE.
  *   - positions, slot_mapping [max_new]: the position and cache row of each new
  *     token, request after request, as mla_cache_append takes them. A refused
  *     request keeps its places there (position 0, slot -1); places past the sum of

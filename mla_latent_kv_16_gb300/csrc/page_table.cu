@@ -177,52 +177,63 @@ __device__ void extend_apply(const ExtendArgs& a, int i, int at, int step, int32
   const ExtendItem it = static_cast<const ExtendItem*>(a.items)[i];
   const int32_t s = a.src[i], d = a.dst[i];
   const int32_t P = a.page_size;
-  bool ok = it.len >= 0;
-  int32_t full = 0, keep = 0, need = 0;
-  if (ok) {
-    full = it.len / P;
-    keep = s != d ? full : (it.len + P - 1) / P;  // the first page that is newly allocated
-    need = static_cast<int32_t>((static_cast<int64_t>(it.len) + it.n_new + P - 1) / P);
-    if (need > keep && static_cast<int64_t>(it.page_at) + (need - keep) > free_total) {
-      ok = false;
-      if (at == 0) flag_error(a.dev_error, MLA_DEVERR_NO_PAGE);
-    }
-  }
   const int64_t width = a.max_pages;
   const int32_t* from = a.block_table + s * width;
   int32_t* to = a.block_table + d * width;
   const int32_t* fresh = a.free_list + it.page_at;  // [need - keep]
-  const bool tail = ok && s != d && it.len % P != 0;
-  auto page_of = [&](int k) -> int32_t {  // of new token k
-    const int32_t page = (it.len + k) / P;
-    return page < keep ? from[page] : fresh[page - keep];
-  };
-  int32_t tail_page = -1, tail_to = -1, e_fresh = -1, e_slot = -1;
-  if (tail && at == 0) tail_page = from[full], tail_to = fresh[0];
-  if (ok && keep + at < need) e_fresh = fresh[at];
-  if (ok && at < it.n_new) e_slot = page_of(at);
-  if (ok && s != d)
-    for (int p0 = at; p0 < keep; p0 += kBatch * step) {  // shared full pages (a given-back page stays none)
-      int32_t e[kBatch];
+  bool ok = it.len >= 0;
+  const bool fork = ok && s != d;
+  int32_t full = 0, keep = 0, need = 0, bad = 0;
+  bool cut = false;  // the source's last page is partly filled: its rows are copied, or new ones follow them
+  if (ok) {
+    full = it.len / P;
+    keep = fork ? full : (it.len + P - 1) / P;  // the first page that is newly allocated
+    need = static_cast<int32_t>((static_cast<int64_t>(it.len) + it.n_new + P - 1) / P);
+    cut = it.len % P != 0 && (fork || it.n_new > 0);
+    if (need > keep && static_cast<int64_t>(it.page_at) + (need - keep) > free_total) bad = MLA_DEVERR_NO_PAGE;
+  }
+  int32_t last = -1, tail_to = -1, e_fresh = -1, e_slot = -1;
+  int32_t shared[kBatch];  // entries at, at + step, ... of the pages that a fork shares (a given-back page stays none)
+  auto load_shared = [&](int p0) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) e[k] = p0 + k * step < keep ? from[p0 + k * step] : -1;
+    for (int k = 0; k < kBatch; ++k) shared[k] = p0 + k * step < keep ? from[p0 + k * step] : -1;
+  };
+  // (no request of the call writes `last`: growths write the pages past it, forks the rows of empty sequences)
+  if (cut) last = from[full];
+  if (bad == 0) {
+    if (fork && cut && at == 0) tail_to = fresh[0];
+    if (keep + at < need) e_fresh = fresh[at];
+    const int32_t page = (it.len + at) / P;
+    if (ok && at < it.n_new && page >= keep) e_slot = fresh[page - keep];
+  }
+  if (fork) load_shared(at);
+  if (cut && (last < 0 || last >= a.num_pages)) bad |= MLA_DEVERR_BAD_PAGE;
+  if (bad != 0) {
+    ok = false;
+    if (at == 0) flag_error(a.dev_error, bad);
+  }
+  // page of new token k: a growth's first tokens go to the last page, the others to new ones
+  auto page_of = [&](int k) -> int32_t {
+    const int32_t page = (it.len + k) / P;
+    return page < keep ? last : (k == at ? e_slot : fresh[page - keep]);
+  };
+  if (ok && fork)
+    for (int p0 = at; p0 < keep; p0 += kBatch * step) {
+      if (p0 > at) load_shared(p0);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (p0 + k * step >= keep) break;
-        if (e[k] >= a.num_pages) flag_error(a.dev_error, MLA_DEVERR_BAD_PAGE);
-        const bool valid = e[k] >= 0 && e[k] < a.num_pages;
-        to[p0 + k * step] = valid ? e[k] : -1;
-        if (valid) atomicAdd(&a.ref_counts[e[k]], 1);
+        if (shared[k] >= a.num_pages) flag_error(a.dev_error, MLA_DEVERR_BAD_PAGE);
+        const bool valid = shared[k] >= 0 && shared[k] < a.num_pages;
+        to[p0 + k * step] = valid ? shared[k] : -1;
+        if (valid) atomicAdd(&a.ref_counts[shared[k]], 1);
       }
     }
   if (at == 0) {
-    if (tail && (tail_page < 0 || tail_page >= a.num_pages)) {
-      tail_page = -1;
-      flag_error(a.dev_error, MLA_DEVERR_BAD_PAGE);
-    }
-    a.copy_src[i] = tail_page;
-    a.copy_dst[i] = tail_page >= 0 ? tail_to : -1;
-    a.copy_rows[i] = tail_page >= 0 ? it.len % P : 0;
+    const bool tail = ok && fork && cut;
+    a.copy_src[i] = tail ? last : -1;
+    a.copy_dst[i] = tail ? tail_to : -1;
+    a.copy_rows[i] = tail ? it.len % P : 0;
     if (ok) a.seq_lens[d] = it.len + it.n_new;
   }
   if (ok)
@@ -232,16 +243,9 @@ __device__ void extend_apply(const ExtendArgs& a, int i, int at, int step, int32
       a.ref_counts[e] = 1;
     }
   for (int k = at; k < it.n_new; k += step) {
-    int64_t slot = -1;
-    if (ok) {
-      const int32_t pos = it.len + k, e = k == at ? e_slot : page_of(k);
-      if (e >= 0 && e < a.num_pages)
-        slot = static_cast<int64_t>(e) * P + pos % P;
-      else
-        flag_error(a.dev_error, MLA_DEVERR_BAD_PAGE);
-    }
-    a.positions[it.token_at + k] = ok ? it.len + k : 0;
-    a.slots[it.token_at + k] = slot;
+    const int32_t pos = it.len + k;
+    a.positions[it.token_at + k] = ok ? pos : 0;
+    a.slots[it.token_at + k] = ok ? static_cast<int64_t>(page_of(k)) * P + pos % P : -1;
   }
 }
 
