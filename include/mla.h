@@ -411,7 +411,9 @@ mla_status_t mla_prefill_window(const void *q_nope, const void *q_rope, const vo
  *   block_table [num_seqs][max_pages_per_seq] int32: physical page of each
  *               logical page, -1 where there is none
  *   seq_lens    [num_seqs] int32: cached tokens (0: the sequence is empty and its
- *               row holds no page)
+ *               row holds no page). A row holds no page past its sequence's last one:
+ *               mla_cache_extend puts its new pages there without looking, and a page
+ *               that was there stays counted
  *   ref_counts  [num_pages] int32, 16-byte aligned: how many rows hold the page;
  *               0 = free. A new pool starts with zeros and a table of -1.
  * Limits: num_seqs <= 32768, num_pages <= 2^30, lists of <= 2^20 entries,
@@ -435,6 +437,10 @@ mla_status_t mla_prefill_window(const void *q_nope, const void *q_rope, const vo
  *     source's page is written or freed. Requests without such a page get -1, -1, 0.
  *   - New pages are the lowest-numbered free ones. A request that needs more
  *     than are left after the earlier requests is refused (MLA_DEVERR_NO_PAGE).
+ *     What the earlier ones ask for counts, whether they get it or not: after a
+ *     request that is refused for its pages every later one that needs a page is
+ *     refused too, and the pages meant for a request that is refused as
+ *     MLA_DEVERR_BAD_PAGE stay free. Requests refused for any other reason count none.
  *   - A request that copies rows of the source's partly filled last page, or puts
  *     new tokens behind them, is refused (MLA_DEVERR_BAD_PAGE) where the row holds
  *     no page of the pool there. An entry of a shared page that lies outside the
@@ -468,8 +474,10 @@ mla_status_t mla_cache_extend(const int32_t *src_seqs, const int32_t *dst_seqs,
  * A pair of two negative pages is no copy, nor is a page onto itself. A page
  * outside the pool or n_rows outside [0, page_size] refuses the pair
  * (MLA_DEVERR_BAD_PAGE). The copies run at the same time, so a pair whose source
- * another pair writes, or whose destination an earlier pair writes, is refused
- * (MLA_DEVERR_CONFLICT); chain such copies over two calls.
+ * is another pair's destination, or whose destination is an earlier pair's, is
+ * refused (MLA_DEVERR_CONFLICT); chain such copies over two calls. For this every
+ * pair of two different pages of the pool counts, whatever its n_rows and whether
+ * it is refused itself or not.
  *   page_size <= 2^20, n_pairs <= 2^20, num_pages <= 2^30
  *   workspace: >= mla_cache_copy_workspace_size(n_pairs, num_pages) bytes, 16-byte
  *              aligned (0 for short lists); nothing in it has to start at zero
