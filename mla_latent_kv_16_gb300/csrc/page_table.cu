@@ -242,8 +242,9 @@ __device__ void extend_apply(const ExtendArgs& a, int i, int at, int step, int32
       to[p] = e;
       a.ref_counts[e] = 1;
     }
-  for (int k = at; k < it.n_new; k += step) {
-    const int32_t pos = it.len + k;
+  // (n_new may come within a step of 2^31: the counter is unsigned)
+  for (uint32_t t = at; t < static_cast<uint32_t>(it.n_new); t += step) {
+    const int32_t k = static_cast<int32_t>(t), pos = it.len + k;
     a.positions[it.token_at + k] = ok ? pos : 0;
     a.slots[it.token_at + k] = ok ? static_cast<int64_t>(page_of(k)) * P + pos % P : -1;
   }

@@ -73,3 +73,21 @@ def test_a_source_whose_last_page_is_full():
     assert int(d.err.item()) == BAD_PAGE
     assert d.table[3].tolist() == [-1] + m.table[1, 1:3].tolist() + [-1] * 5
     assert int(d.lens[3]) == 12 and d.refs[m.table[1, 1:3].tolist()].tolist() == [2, 2]
+
+
+def test_the_longest_list_of_new_tokens():
+    """A refused request owns its places whatever their number: 2^31 - 1 of them, where a 32-bit signed
+    count of steps of thousands would pass its end."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 26 GB")
+    from mla_latent_kv_16_gb300 import capi
+    m = Model(2, 4, 8, 4)
+    d = Device(m)
+    pos = torch.full((INT_MAX,), -7, dtype=torch.int32, device="cuda")
+    slot = torch.full((INT_MAX,), -7, dtype=torch.int64, device="cuda")
+    one, n = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), INT_MAX, dtype=torch.int32, device="cuda")
+    capi.mla_cache_extend(one, one, n, d.table, d.lens, d.refs, 4, positions=pos, slots=slot, dev_error=d.err)
+    assert int(d.err.item()) == BAD_SEQLEN
+    assert int(pos.max()) == int(pos.min()) == 0 and int(slot.max()) == int(slot.min()) == -1
+    m.err = BAD_SEQLEN
+    same(m, d)
