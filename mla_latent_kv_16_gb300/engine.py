@@ -140,12 +140,15 @@ class MLADecodeLayer:
 
     # ------------------------------------------------------------------ sequences and pages
 
-    def _page_state(self, stream):
-        """Reference counts of the block table's pages and the calls' buffers, made on the
-        call's stream when the first page call needs them."""
+    def prepare_pages(self, stream=None):
+        """Makes the page calls' buffers on the call's stream and counts the block table's pages
+        (ref_counts), once. The first page call does it; call it before capturing that one,
+        since a graph would count anew at every replay."""
         if hasattr(self, "ref_counts"):
             return
         with capi.on_stream(stream):
+            if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("prepare_pages() has to run before a page call is captured")
             i32 = dict(dtype=torch.int32, device=self.device)
             n, moves = self.block_table.shape[0], min(max(1, self.num_pages // 2), capi.MAX_LIST)
             self._lists = torch.empty(3, n, **i32)
@@ -156,8 +159,8 @@ class MLADecodeLayer:
                        capi.mla_cache_compact_workspace_size(self.num_pages),
                        capi.mla_cache_copy_workspace_size(max(n, moves), self.num_pages))
             self._page_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            held = self.block_table[self.block_table >= 0].long()
-            self.ref_counts = torch.bincount(held, minlength=self.num_pages).to(torch.int32)
+            held = self.block_table[self.block_table >= 0]
+            self.ref_counts = torch.bincount(held.long(), minlength=self.num_pages).to(torch.int32)
 
     def extend(self, src_seqs, dst_seqs, n_new, positions, slots, stream=None):
         """Fork and grow: sequence dst_seqs[i] becomes sequence src_seqs[i] with room for
@@ -165,7 +168,7 @@ class MLADecodeLayer:
         most one entry per sequence. Fills positions (int32) and slots (int64) of the
         new tokens, request after request, as step() and append() take them, and copies
         the forks' partly filled pages in this layer's pool."""
-        self._page_state(stream)
+        self.prepare_pages(stream)
         n = src_seqs.numel()
         lists = [self._lists[k][:n] for k in range(3)]
         capi.mla_cache_extend(src_seqs, dst_seqs, n_new, self.block_table, self.seq_lens, self.ref_counts, self.P,
@@ -176,7 +179,7 @@ class MLADecodeLayer:
 
     def free(self, seqs, stream=None):
         """The listed sequences end: their pages go back and their rows are empty."""
-        self._page_state(stream)
+        self.prepare_pages(stream)
         capi.mla_cache_free(seqs, self.block_table, self.seq_lens, self.ref_counts, self.P, dev_error=self.dev_error,
                             stream=stream)
 
@@ -185,14 +188,14 @@ class MLADecodeLayer:
         step: with several queries per sequence, the step's own earlier ones reach further back."""
         if self.window < 1:
             raise ValueError("evict() needs a layer with a window")
-        self._page_state(stream)
+        self.prepare_pages(stream)
         capi.mla_cache_free(self._all_seqs, self.block_table, self.seq_lens, self.ref_counts, self.P, self.window,
                             self.sinks, dev_error=self.dev_error, stream=stream)
 
     def compact(self, stream=None):
         """Moves the live pages to the front of the pool (at most 2^20 of them in a call). Returns
         the device tensor (live pages, pages at the front that hold them)."""
-        self._page_state(stream)
+        self.prepare_pages(stream)
         src, dst = self._moves[0], self._moves[1]
         capi.mla_cache_compact(self.block_table, self.ref_counts, src, dst, self._stats, workspace=self._page_ws,
                                dev_error=self.dev_error, stream=stream)

@@ -79,3 +79,29 @@ def test_a_serving_loop_without_a_window(cache, heads, page, splits):
     assert stats.tolist() == [n, n]
     life.check("compacted")
     assert layer.device_error() & ~2 == 0  # (2: the empty sequences of the batch)
+
+
+def test_the_first_page_call_captured():
+    """A page state that does not exist yet cannot be made inside a capture: the call is refused before
+    anything is enqueued, the capture stays usable, and after prepare_pages() it is captured."""
+    layer = make_layer("bf16", 16, 2, 16, pages=12, width=5, max_pos=80, window=20, sinks=1)
+    every = torch.arange(2, dtype=torch.int32, device="cuda")
+    grow = torch.full((2,), 17, dtype=torch.int32, device="cuda")
+    pos, slots = torch.empty(34, dtype=torch.int32, device="cuda"), torch.empty(34, dtype=torch.int64, device="cuda")
+    calls = [lambda: layer.extend(every, every, grow, pos, slots), lambda: layer.free(every), layer.evict, layer.compact]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call in calls:
+            with pytest.raises(RuntimeError, match="prepare_pages"):
+                call()
+    layer.prepare_pages()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.extend(every, every, grow, pos, slots)
+    for n in (1, 2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert layer.seq_lens.tolist() == [17 * n] * 2
+        assert int((layer.ref_counts == 1).sum()) == 2 * -(-17 * n // 16) and int(layer.ref_counts.sum()) == int((layer.block_table >= 0).sum())
+    assert layer.device_error() == 0
