@@ -143,7 +143,7 @@ class MLADecodeLayer:
     def prepare_pages(self, stream=None):
         """Makes the page calls' buffers on the call's stream and counts the block table's pages
         (ref_counts), once. The first page call does it; call it before capturing that one,
-        since a graph would count anew at every replay."""
+        since a graph would count anew at every replay. Entries outside the pool are nobody's pages."""
         if hasattr(self, "ref_counts"):
             return
         with capi.on_stream(stream):
@@ -159,7 +159,7 @@ class MLADecodeLayer:
                        capi.mla_cache_compact_workspace_size(self.num_pages),
                        capi.mla_cache_copy_workspace_size(max(n, moves), self.num_pages))
             self._page_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            held = self.block_table[self.block_table >= 0]
+            held = self.block_table[(self.block_table >= 0) & (self.block_table < self.num_pages)]
             self.ref_counts = torch.bincount(held.long(), minlength=self.num_pages).to(torch.int32)
 
     def extend(self, src_seqs, dst_seqs, n_new, positions, slots, stream=None):

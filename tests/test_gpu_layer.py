@@ -105,3 +105,17 @@ def test_the_first_page_call_captured():
         assert layer.seq_lens.tolist() == [17 * n] * 2
         assert int((layer.ref_counts == 1).sum()) == 2 * -(-17 * n // 16) and int(layer.ref_counts.sum()) == int((layer.block_table >= 0).sum())
     assert layer.device_error() == 0
+
+
+def test_pages_outside_the_pool_are_not_handed_out():
+    """A table with entries past the pool: the pages that extend() hands out are the pool's."""
+    table = torch.full((2, 6), -1, dtype=torch.int32)
+    table[1, :3] = torch.tensor([3, 5000, 1])
+    layer = make_layer("bf16", 16, 2, 16, pages=5, width=6, max_pos=96, table=table,
+                       lens=torch.tensor([0, 48], dtype=torch.int32))
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pos, slots = torch.empty(40, dtype=torch.int32, device="cuda"), torch.empty(40, dtype=torch.int64, device="cuda")
+    layer.extend(one, one, one + 40, pos, slots)
+    assert layer.block_table[0].tolist() == [0, 2, 4, -1, -1, -1] and layer.device_error() == 0
+    layer.extend(one, one, one + 9, pos, slots)  # none is left
+    assert layer.block_table[0].tolist() == [0, 2, 4, -1, -1, -1] and layer.device_error() == 64

@@ -43,3 +43,17 @@ def test_workspace_is_sized_by_the_table(capi, cache, heads, splits, window):
     assert want > 1
     assert layer.splits == want
     assert layer.workspace.numel() >= need
+
+
+def test_page_state_counts_the_pool_only(capi):
+    """Entries outside the pool are nobody's pages: the counts are as many as the pool has pages,
+    or new pages would be handed out behind its end."""
+    table = torch.tensor([[0, 2, -1, -1], [3, 9, 2 ** 31 - 1, -2 ** 31], [2, 10, 8, -1]], dtype=torch.int32)
+    layer = make(3, 16, 4, heads=16, table=table, pages_each=3)
+    assert layer.num_pages == 9
+    layer.prepare_pages()
+    assert layer.ref_counts.dtype == torch.int32
+    assert layer.ref_counts.tolist() == [1, 0, 2, 1, 0, 0, 0, 0, 1]
+    counts = layer.ref_counts
+    layer.prepare_pages()  # once
+    assert layer.ref_counts is counts
