@@ -42,6 +42,8 @@ class MLADecodeLayer:
         pages of the pool beyond the workload's, for extend(). max_pos: positions of the
         RoPE table beyond the workload's longest sequence. block_table may be wider than
         the workload's sequences need."""
+        if window < 0 or sinks < 0:
+            raise ValueError("window and sinks must not be negative")
         self.w = w
         self.device = torch.device(device)
         self.H = w.heads

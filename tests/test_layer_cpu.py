@@ -57,3 +57,10 @@ def test_page_state_counts_the_pool_only(capi):
     counts = layer.ref_counts
     layer.prepare_pages()  # once
     assert layer.ref_counts is counts
+
+
+@pytest.mark.parametrize("kw", [dict(window=-1), dict(sinks=-1), dict(window=5, sinks=-3)])
+def test_negative_window_or_sinks_are_refused(capi, kw):
+    """A negative window is none of the masks there are (0 stands for every earlier token)."""
+    with pytest.raises(ValueError, match="negative"):
+        make(2, 16, 2, heads=16, **kw)
