@@ -1,6 +1,7 @@
 // C ABI entry points (include/mla.h): argument validation, split policy and
 // dispatch to the sm_103a kernels. No allocation happens here; every buffer is
 // the caller's.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -11,15 +12,15 @@
 namespace mla {
 
 int device_sm_count() {
-  static int cached[64] = {0};
+  static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (cached[dev] == 0) {
-    int n = 0;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    cached[dev] = n;
+    cached[dev].store(n, std::memory_order_relaxed);
   }
-  return cached[dev];
+  return n;
 }
 
 namespace {

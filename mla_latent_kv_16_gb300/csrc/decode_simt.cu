@@ -20,6 +20,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 
 namespace mla {
@@ -457,22 +458,10 @@ __global__ void __launch_bounds__(256) combine_many_kernel(DecodeArgs a) {
   combine_store<T>(a, bj, h, lane, acc, none, mx, tot);
 }
 
-// Opt the kernel into its dynamic shared memory once per device (a host call
-// that costs microseconds, kept out of every launch).
-template <typename K>
-cudaError_t ensure_smem(K kernel, size_t bytes, int& done_for) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || done_for == dev) return e;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess) done_for = dev;
-  return e;
-}
-
 template <typename T, int kCache, bool kWin>
 cudaError_t launch_decode_w(const DecodeArgs& a, cudaStream_t s) {
-  static int done_for = -1;
-  const cudaError_t e = ensure_smem(decode_simt_kernel<T, kCache, kWin>, kSimtSmem, done_for);
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(kSimtSmem, decode_simt_kernel<T, kCache, kWin>);
   if (e != cudaSuccess) return e;
   dim3 grid(a.num_splits, (a.heads + kHG - 1) / kHG, a.batch * a.q_len);
   return launch_pdl(decode_simt_kernel<T, kCache, kWin>, grid, dim3(256), kSimtSmem, s, a);

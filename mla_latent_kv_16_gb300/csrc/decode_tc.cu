@@ -79,6 +79,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 #include "tc_ptx.cuh"
 
@@ -1119,21 +1120,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for(kFp8), 1
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 }  // namespace
 
 bool decode_tc_supported(const DecodeArgs& a) {
@@ -1204,22 +1190,10 @@ cudaError_t launch_decode_tc(const DecodeArgs& args, cudaStream_t s) {
   a.box_rows = kTileTok;
   if (a.window > 0)
     while (a.page_size % a.box_rows != 0) a.box_rows >>= 1;  // (a multiple of 8: decode_tc_supported)
-  static int attr_set_for_device = -1;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  if (attr_set_for_device != dev) {
-    const auto opt_in = [](auto kernel) {
-      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-    };
-    cudaError_t e = opt_in(decode_tc_kernel<false, 0>);
-    if (e == cudaSuccess) e = opt_in(decode_tc_kernel<true, 0>);
-    if (e == cudaSuccess) e = opt_in(decode_tc_kernel<false, 1>);
-    if (e == cudaSuccess) e = opt_in(decode_tc_kernel<true, 1>);
-    if (e == cudaSuccess) e = opt_in(decode_tc_kernel<false, 2>);
-    if (e == cudaSuccess) e = opt_in(decode_tc_kernel<true, 2>);
-    if (e != cudaSuccess) return e;
-    attr_set_for_device = dev;
-  }
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(kSmemBytes, decode_tc_kernel<false, 0>, decode_tc_kernel<true, 0>, decode_tc_kernel<false, 1>,
+                               decode_tc_kernel<true, 1>, decode_tc_kernel<false, 2>, decode_tc_kernel<true, 2>);
+  if (e != cudaSuccess) return e;
   const bool fp8 = a.cache_dtype == MLA_E4M3;
   CUtensorMap map, qmap, rmap, pmap;
   const uint64_t q_rows = static_cast<uint64_t>(a.batch) * a.q_len * a.heads;

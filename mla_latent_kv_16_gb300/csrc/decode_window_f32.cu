@@ -30,6 +30,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 
 namespace mla {
@@ -249,16 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_window_f32_kernel(const De
 }  // namespace
 
 cudaError_t launch_decode_window_f32(const DecodeArgs& a, cudaStream_t s) {
-  static int attr_dev = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(sizeof(F32Smem), decode_window_f32_kernel);
   if (e != cudaSuccess) return e;
-  if (attr_dev != dev) {
-    e = cudaFuncSetAttribute(decode_window_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sizeof(F32Smem)));
-    if (e != cudaSuccess) return e;
-    attr_dev = dev;
-  }
   const dim3 grid(a.num_splits, (a.heads + kHeads - 1) / kHeads, a.batch * a.q_len);
   return launch_pdl(decode_window_f32_kernel, grid, dim3(kThreads), sizeof(F32Smem), s, a);
 }

@@ -29,6 +29,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 #include "tc_ptx.cuh"
 
@@ -278,25 +279,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 ex_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
 // [rows][cols] bf16 with row stride `stride` elements, 64 x box_rows boxes, 128-byte swizzle
 bool ex_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows) {
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {stride * 2};
   const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return ex_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -304,7 +293,7 @@ bool ex_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint6
 }  // namespace
 
 cudaError_t launch_expand(const ExpandArgs& x, cudaStream_t s) {
-  if (ex_encoder() == nullptr) return cudaErrorNotSupported;
+  if (tensor_map_encoder() == nullptr) return cudaErrorNotSupported;
   const uint64_t hd = static_cast<uint64_t>(x.heads) * 128;
   ExMaps maps;
   ExArgs a{};
@@ -334,15 +323,9 @@ cudaError_t launch_expand(const ExpandArgs& x, cudaStream_t s) {
   const int64_t row_tiles = (n[0] + kPairRows - 1) / kPairRows + (n[1] + kPairRows - 1) / kPairRows;
   a.units = static_cast<int32_t>(row_tiles * 2 * a.out_tiles);
   a.dev_error = x.dev_error;
-  static int attr_dev = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(kExSmemBytes, expand_kernel);
   if (e != cudaSuccess) return e;
-  if (attr_dev != dev) {
-    e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kExSmemBytes));
-    if (e != cudaSuccess) return e;
-    attr_dev = dev;
-  }
   const int pairs = device_sm_count() / 2;
   const unsigned grid = 2u * static_cast<unsigned>(a.units < pairs ? a.units : pairs);
   return launch_pdl(expand_kernel, dim3(grid), dim3(kExThreads), kExSmemBytes, s, maps, a);

@@ -27,6 +27,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 #include "tc_ptx.cuh"
 
@@ -389,21 +390,6 @@ __global__ void __launch_bounds__(256) linear_reduce_kernel(LinearArgs p) {
 
 // ------------------------------------------------------------------ host side
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 // 2D map over a [rows][cols] bf16 matrix (row stride `stride` elements, 0 =
 // cols), boxes of 64 columns x box_rows.
 bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
@@ -412,7 +398,7 @@ bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, ui
   const cuuint64_t strides[1] = {(stride != 0 ? stride : cols) * 2};
   const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -508,7 +494,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s, bool reduce) {
     if (a.act == MLA_F32) return launch_pdl(linear_simt_kernel<float>, grid, dim3(256), 0, s, a);
     return launch_pdl(linear_simt_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a);
   }
-  if (encoder() == nullptr) return cudaErrorNotSupported;
+  if (tensor_map_encoder() == nullptr) return cudaErrorNotSupported;
   const LinearPlan pl = plan_tc(a.n_tokens, a.n_out, a.n_in);
   if (pl.splits != a.k_splits || (pl.splits > 1 && a.part == nullptr)) return cudaErrorInvalidValue;
   CUtensorMap am, bm;
@@ -517,15 +503,9 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s, bool reduce) {
       !encode_2d(&bm, a.x, static_cast<uint64_t>(a.n_tokens), static_cast<uint64_t>(a.n_in),
                  pl.tm ? 128u : static_cast<uint32_t>(pl.n_tile), static_cast<uint64_t>(a.x_stride)))
     return cudaErrorInvalidValue;
-  static int attr_dev = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in(220 * 1024, linear_tc_kernel);
   if (e != cudaSuccess) return e;
-  if (attr_dev != dev) {
-    e = cudaFuncSetAttribute(linear_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
-    if (e != cudaSuccess) return e;
-    attr_dev = dev;
-  }
   e = launch_pdl(linear_tc_kernel, dim3(pl.grid), dim3(kThreads), pl.smem, s, am, bm, a, pl.n_tile, pl.stages,
                  pl.acc_cols, pl.units, pl.tm ? 1 : 0);
   if (e != cudaSuccess || a.part == nullptr || !reduce) return e;

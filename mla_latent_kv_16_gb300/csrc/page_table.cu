@@ -22,6 +22,7 @@
 // large compaction took 18.5 and 15 with three launches, 11.3 and 11.5 with the
 // requests checked before the count and every load awaited by itself.
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 #include "tc_ptx.cuh"
 
@@ -525,18 +526,9 @@ cudaError_t launch_extend(ExtendArgs a, void* workspace, cudaStream_t s) {
   a.free_total = reinterpret_cast<int32_t*>(ws + align256(static_cast<size_t>(a.n) * sizeof(ExtendItem)));
   a.free_list = a.free_total + 64;
   const size_t smem = static_cast<size_t>(a.num_seqs) * sizeof(int32_t);
-  static int attr_dev = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in(kMaxTableSeqs * sizeof(int32_t), extend_plan_kernel<true>, extend_plan_kernel<false>);
   if (e != cudaSuccess) return e;
-  if (attr_dev != dev) {
-    const int most = kMaxTableSeqs * static_cast<int>(sizeof(int32_t));
-    e = cudaFuncSetAttribute(extend_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(extend_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess) return e;
-    attr_dev = dev;
-  }
   if (static_cast<int64_t>(a.n) * a.max_pages + a.max_new <= kFusedWork)
     return launch_pdl(extend_plan_kernel<true>, dim3(kPlanCtas), dim3(kPlanThreads), smem, s, a);
   e = launch_pdl(extend_plan_kernel<false>, dim3(kPlanCtas), dim3(kPlanThreads), smem, s, a);

@@ -40,6 +40,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 #include "tc_ptx.cuh"
 
@@ -404,28 +405,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const __gri
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 pf_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 // [rows][cols] bf16 with row stride `stride` elements, 64 x 128 boxes, 128-byte swizzle
 bool pf_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t stride) {
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {stride * 2};
   const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kRowsTile)};
   const cuuint32_t estr[2] = {1, 1};
-  return pf_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -437,7 +423,7 @@ size_t prefill_workspace_bytes(int32_t n_tokens, int32_t heads) {
   return 2 * one;
 }
 
-bool prefill_supported() { return pf_encoder() != nullptr; }
+bool prefill_supported() { return tensor_map_encoder() != nullptr; }
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s) {
   const int64_t T = a.n_tokens, H = a.heads;
@@ -459,16 +445,9 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s) {
       !pf_map(&maps.kr, a.rows, static_cast<uint64_t>(T), 576, 576) ||
       !pf_map(&maps.v, a.v, static_cast<uint64_t>(T), static_cast<uint64_t>(H * 128), static_cast<uint64_t>(H * 128)))
     return cudaErrorInvalidValue;
-  static int attr_dev = -1;
-  int dev = 0;
-  e = cudaGetDevice(&dev);
+  static SmemOptIn opt_in;
+  e = opt_in(kPfSmemBytes, prefill_attn_kernel);
   if (e != cudaSuccess) return e;
-  if (attr_dev != dev) {
-    e = cudaFuncSetAttribute(prefill_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kPfSmemBytes));
-    if (e != cudaSuccess) return e;
-    attr_dev = dev;
-  }
   const int64_t n_qt = (a.n_queries + kRowsTile - 1) / kRowsTile;
   const int64_t blocks = n_qt * H;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;

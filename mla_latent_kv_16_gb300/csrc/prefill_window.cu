@@ -55,6 +55,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 #include "tc_ptx.cuh"
 
@@ -606,25 +607,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 pw_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
 // [rows][cols] bf16 with row stride `stride` elements, 64 x 128 boxes, 128-byte swizzle
 bool pw_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t stride) {
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {stride * 2};
   const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kTile)};
   const cuuint32_t estr[2] = {1, 1};
-  return pw_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -643,7 +632,7 @@ PrefillWindow prefill_window_regions(int32_t n_tokens, int32_t n_queries, int32_
 }
 
 cudaError_t launch_prefill_window(const PrefillArgs& a, cudaStream_t s) {
-  if (pw_encoder() == nullptr) return cudaErrorNotSupported;
+  if (tensor_map_encoder() == nullptr) return cudaErrorNotSupported;
   const PrefillWindow w = prefill_window_regions(a.n_tokens, a.n_queries, a.window, a.sinks);
   cudaError_t e = launch_expand(
       ExpandArgs{a.rows, a.w_uk, a.w_uv, a.k_nope, a.v, w.lo, w.rows_a, w.rows_b, a.heads, a.dev_error}, s);
@@ -664,16 +653,9 @@ cudaError_t launch_prefill_window(const PrefillArgs& a, cudaStream_t s) {
       !region(1, w.lo, w.rows_b, w.rows_a) || (w.rows_a > 0 && !region(0, 0, w.rows_a, 0)))
     return cudaErrorInvalidValue;
   if (w.rows_a == 0) maps.k[0] = maps.k[1], maps.kr[0] = maps.kr[1], maps.v[0] = maps.v[1];
-  static int attr_dev = -1;
-  int dev = 0;
-  e = cudaGetDevice(&dev);
+  static SmemOptIn opt_in;
+  e = opt_in(kPwSmemBytes, prefill_window_kernel);
   if (e != cudaSuccess) return e;
-  if (attr_dev != dev) {
-    e = cudaFuncSetAttribute(prefill_window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kPwSmemBytes));
-    if (e != cudaSuccess) return e;
-    attr_dev = dev;
-  }
   const int32_t n_qt = (a.n_queries + kTile - 1) / kTile;
   const int32_t units = n_qt * a.heads;  // at most 2^13 x 128
   const int32_t sms = device_sm_count();

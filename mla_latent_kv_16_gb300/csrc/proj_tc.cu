@@ -21,6 +21,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "launchers.h"
 #include "tc_ptx.cuh"
 
@@ -365,28 +366,13 @@ __global__ void __launch_bounds__(kMpThreads) out_proj_merge_kernel(const __grid
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 // 2D map over a [rows][cols] bf16 matrix with boxes of 64 columns x box_rows.
 bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols * 2};
   const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -397,14 +383,14 @@ bool encode_3d(CUtensorMap* m, const void* ptr, uint64_t tokens, uint64_t heads,
   const cuuint64_t strides[2] = {width * 2, heads * width * 2};
   const cuuint32_t box[3] = {64, 1, box_tok};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int kKind>
 cudaError_t launch_proj(const ProjArgs& a, cudaStream_t s) {
-  if (a.act != MLA_BF16 || encoder() == nullptr) return cudaErrorNotSupported;
+  if (a.act != MLA_BF16 || tensor_map_encoder() == nullptr) return cudaErrorNotSupported;
   if (a.n_tokens == 0) return cudaSuccess;
   const int n_tile = a.n_tokens >= kMaxTok ? kMaxTok : ((a.n_tokens + 15) / 16) * 16;
   uint32_t cols = 32;
@@ -424,15 +410,9 @@ cudaError_t launch_proj(const ProjArgs& a, cudaStream_t s) {
     ok = encode_2d(&am, a.w, static_cast<uint64_t>(a.heads) * kDV, kDC, 128) &&
          encode_3d(&bm, a.x, a.n_tokens, a.heads, kDC, n_tile);
   if (!ok) return cudaErrorInvalidValue;
-  static int attr_dev = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(200 * 1024, proj_tc_kernel<kKind>);
   if (e != cudaSuccess) return e;
-  if (attr_dev != dev) {
-    e = cudaFuncSetAttribute(proj_tc_kernel<kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    if (e != cudaSuccess) return e;
-    attr_dev = dev;
-  }
   const dim3 grid(a.heads, kKind == 0 ? kDC / 128 : 1, (a.n_tokens + kMaxTok - 1) / kMaxTok);
   return launch_pdl(proj_tc_kernel<kKind>, grid, dim3(kThreads), smem, s, am, bm, a, n_tile, stages, cols);
 }
@@ -443,7 +423,7 @@ cudaError_t launch_absorb_tc(const ProjArgs& a, cudaStream_t s) { return launch_
 cudaError_t launch_out_proj_tc(const ProjArgs& a, cudaStream_t s) { return launch_proj<1>(a, s); }
 
 bool out_proj_merge_supported(int32_t heads, int32_t splits, mla_dtype_t act) {
-  return act == MLA_BF16 && heads >= 1 && splits >= 2 && splits <= 4 && encoder() != nullptr;
+  return act == MLA_BF16 && heads >= 1 && splits >= 2 && splits <= 4 && tensor_map_encoder() != nullptr;
 }
 
 cudaError_t launch_out_proj_merge_tc(const MergeProjArgs& a, cudaStream_t s) {
@@ -455,17 +435,9 @@ cudaError_t launch_out_proj_merge_tc(const MergeProjArgs& a, cudaStream_t s) {
   const size_t smem = 1024 + static_cast<size_t>(kDC / kChunkK) * (kABytes + n_tile * 128) + sizeof(MergeProjCtl);
   CUtensorMap am;
   if (!encode_2d(&am, a.w, static_cast<uint64_t>(a.heads) * kDV, kDC, 128)) return cudaErrorInvalidValue;
-  static int attr_dev = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(200 * 1024, out_proj_merge_kernel<2>, out_proj_merge_kernel<3>, out_proj_merge_kernel<4>);
   if (e != cudaSuccess) return e;
-  if (attr_dev != dev) {
-    for (auto fn : {out_proj_merge_kernel<2>, out_proj_merge_kernel<3>, out_proj_merge_kernel<4>}) {
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-      if (e != cudaSuccess) return e;
-    }
-    attr_dev = dev;
-  }
   const dim3 grid(a.heads, 1, (a.n_tokens + kMpTok - 1) / kMpTok);
   switch (a.num_splits) {
     case 2: return launch_pdl(out_proj_merge_kernel<2>, grid, dim3(kMpThreads), smem, s, am, a, n_tile, cols);
