@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeArgs a) {
   }
 }
 
-constexpr int kFewSplits = 2;
+constexpr int kThreeRows = 24;     // rows per SM from which three splits merge as two do
 constexpr int kCombineWarps = 16;  // heads per CTA of the split merge
 
 // The merged row of (query bj, head h): this lane's 16 columns of u = acc / sum,
@@ -272,15 +272,17 @@ __device__ __forceinline__ void combine_start(const DecodeArgs& a) {
 // memory round trip. A split whose lse is -inf is selected out, never multiplied
 // (its partial may hold anything).
 //
-// Two splits (the common case): one warp per (query, head), each lane with 16
-// consecutive columns of the 512, kCombineWarps heads per CTA: few CTAs, two of
-// which fit an SM (48 registers), so that the whole grid is resident (one wave for
-// the DeepSeek-V3-shaped batch) and has let the next kernel launch within a
-// fraction of a microsecond. (Four warps per row, as below, lose 1 to 2 us of 30 to
-// 63 at 24 and 32 queries of 128 heads and win 1 us of 27 at 8.)
-template <typename T>
-__global__ void __launch_bounds__(32 * kCombineWarps, 2) combine_few_kernel(DecodeArgs a) {
-  constexpr int kS = kFewSplits;
+// Two splits (the common case), and three of many rows: one warp per (query, head),
+// each lane with 16 consecutive columns of the 512, kCombineWarps heads per CTA: few
+// CTAs, two of which fit an SM at two splits (48 registers), so that the whole grid is
+// resident (one wave for the DeepSeek-V3-shaped batch) and has let the next kernel
+// launch within a fraction of a microsecond. (Four warps per row, as below, lose 1 to
+// 2 us of 30 to 63 at 24 and 32 queries of 128 heads and win 1 us of 27 at 8. At three
+// splits the two are even at 28 queries of 128 heads, 24 rows an SM: four warps win 2
+// us of 25 at 8 queries and 0.5 of 20 at 24, and lose 1.2 of 54 at 36 and 3.5 of 90 at
+// 100. At four splits four warps win at any number.)
+template <typename T, int kS>
+__global__ void __launch_bounds__(32 * kCombineWarps, kS == 2 ? 2 : 1) combine_few_kernel(DecodeArgs a) {
   combine_start(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.x * kCombineWarps + warp, bj = blockIdx.y;
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 2) combine_few_kernel(Deco
   combine_store<T>(a, bj, h, lane, acc, none, mx, sum);
 }
 
-// More splits (kFewSplits < S <= kManySplits): the same sums in the same order, with
+// More splits (up to kManySplits): the same sums in the same order, with
 // four warps per (query, head), each lane with four consecutive columns, which leaves
 // registers for eight splits. (One warp per row, with groups of four splits from 5 on:
 // 2.6 us more at 8 queries of 128 heads and 3 or 6 splits, 0.6 to 4.7 at 24 queries.)
@@ -500,9 +502,13 @@ cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
   }
   const dim3 grid((a.heads + kCombineWarps - 1) / kCombineWarps, a.batch * a.q_len), block(32 * kCombineWarps);
   const dim3 grid4((a.heads * kRowWarps + kCombineWarps - 1) / kCombineWarps, a.batch * a.q_len);
-  if (a.num_splits == kFewSplits) {
-    if (a.act == MLA_F32) return launch_pdl(combine_few_kernel<float>, grid, block, 0, s, a);
-    return launch_pdl(combine_few_kernel<__nv_bfloat16>, grid, block, 0, s, a);
+  if (a.num_splits == 2) {
+    if (a.act == MLA_F32) return launch_pdl(combine_few_kernel<float, 2>, grid, block, 0, s, a);
+    return launch_pdl(combine_few_kernel<__nv_bfloat16, 2>, grid, block, 0, s, a);
+  }
+  if (a.num_splits == 3 && static_cast<int64_t>(a.batch) * a.q_len * a.heads >= int64_t{kThreeRows} * device_sm_count()) {
+    if (a.act == MLA_F32) return launch_pdl(combine_few_kernel<float, 3>, grid, block, 0, s, a);
+    return launch_pdl(combine_few_kernel<__nv_bfloat16, 3>, grid, block, 0, s, a);
   }
   if (a.act == MLA_F32) return launch_pdl(combine_kernel<float>, grid4, block, 0, s, a);
   return launch_pdl(combine_kernel<__nv_bfloat16>, grid4, block, 0, s, a);
