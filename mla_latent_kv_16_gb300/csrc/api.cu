@@ -206,16 +206,20 @@ mla_status_t decode_run(DecodeArgs& a, void* workspace, cudaStream_t s, bool mer
   a.part_lse = workspace != nullptr
                    ? reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(rows * 512 * sizeof(float)))
                    : nullptr;
-  a.spread = false;
+  a.next_start = kNextEarly;
   cudaError_t e;
   const bool tc = a.window > 0 ? use_tc_window(a.page_size, a.act, a.cache_dtype)
                                : use_tc_decode(a.heads, a.page_size, a.act, a.cache_dtype);
-  if (tc && decode_tc_supported(a))
+  if (tc && decode_tc_supported(a)) {
+    const int64_t ctas = 2 * static_cast<int64_t>(a.batch) * a.q_len * a.num_splits;
+    if (a.cache_dtype == MLA_E4M3 && a.window == 0 && a.num_splits >= 3 && a.num_splits <= 8 &&
+        3 * ctas <= 2 * device_sm_count())
+      a.next_start = kNextMerged;
     e = launch_decode_tc(a, s);
-  else if (a.window > 0 && a.cache_dtype == MLA_F32)
+  } else if (a.window > 0 && a.cache_dtype == MLA_F32)
     e = launch_decode_window_f32(a, s);
   else {
-    a.spread = true;
+    a.next_start = kNextMerging;
     e = launch_decode_simt(a, s);
   }
   if (e != cudaSuccess) return MLA_ERR_CUDA;

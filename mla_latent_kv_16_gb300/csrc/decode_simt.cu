@@ -249,20 +249,23 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, int bj, int h
   if (lane == 0 && a.lse_out != nullptr) a.lse_out[row] = none ? -CUDART_INF_F : mx + logf(sum);
 }
 
-// A merge behind decode_simt_kernel lets the next kernel launch only once the decode is
-// done. Launched earlier, the next call's decode would find the SMs half taken by this
-// one's and by the waiting merge, and its CTAs, of which an SM holds several, would pile
-// up on the others: called back to back, bf16, 16 heads, 8 sequences of 3000, 303 us by
-// itself and up to 429 with 3 splits, 194 and 302 with 5. The other decode kernels fill
-// an SM with one CTA, and the next one's set-up gains by starting early.
+// When the next kernel may start. It comes early by default: most decode kernels fill an
+// SM with one CTA, and the next one's set-up gains by starting early. Two decodes are
+// slower when the one before them and its merge still hold part of the SMs, so that
+// their CTAs crowd on the others:
+// - decode_simt_kernel, of which an SM holds several CTAs: the next kernel starts when the
+//   merge runs (called back to back, bf16, 16 heads, 8 sequences of 3000: 303 us by itself
+//   and up to 429 with 3 splits, 194 and 302 with 5);
+// - the E4M3 pair kernel, with 3 to 8 splits that leave a third of the SMs free: the next
+//   kernel starts when the merge is done (back to back, 8 sequences of 8000: 3 splits 106
+//   to 113 us for 89, 4 splits 91 to 98 for 75, 12 sequences and 3 splits 125 for 104; with
+//   the absorption before and the projection behind it 128 for 117, 116 for 104, 152 for
+//   139). Where the SMs are full it would cost the kernel behind a merge 1.7 us; the short
+//   splits of a window are within 0.4 us either way and stay early.
 __device__ __forceinline__ void combine_start(const DecodeArgs& a) {
-  if (a.spread) {
-    pdl_wait();
-    pdl_trigger();
-  } else {
-    pdl_trigger();
-    pdl_wait();
-  }
+  if (a.next_start == kNextEarly) pdl_trigger();
+  pdl_wait();
+  if (a.next_start == kNextMerging) pdl_trigger();
 }
 
 // Split-KV merge ("Model Architecture Driving Inference Systems" §4.1, split

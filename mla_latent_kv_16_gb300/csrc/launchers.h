@@ -192,6 +192,7 @@ struct FrontArgs {
 size_t front_workspace_bytes(int32_t n_tokens, int32_t d_model, int32_t d_cq, int32_t heads, mla_dtype_t act);
 cudaError_t launch_front(const FrontArgs& f, cudaStream_t s);
 
+constexpr int32_t kNextEarly = 0, kNextMerging = 1, kNextMerged = 2;  // DecodeArgs::next_start
 struct DecodeArgs {
   const void* q_lat;
   const void* q_rope;
@@ -218,7 +219,7 @@ struct DecodeArgs {
   int32_t window;         // 0: every earlier token is visible; else the last `window` and the first `sinks`
   int32_t sinks;
   int32_t box_rows;       // set by launch_decode_tc: rows of a TMA box (64 without a window)
-  bool spread;         // the merge holds the next kernel back until it runs itself (see combine_start)
+  int32_t next_start;     // when the merge lets the next kernel start (see combine_start)
 };
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s);
