@@ -473,7 +473,10 @@ def on_stream(stream):
     that their memory is not handed to another one while the call may still use it."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    if not hasattr(stream, "cuda_stream"):
+        # (an ExternalStream of handle 0 would be a new stream, not the default one)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _new_scratch(need: int, device):
