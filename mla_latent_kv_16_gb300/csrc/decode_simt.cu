@@ -254,8 +254,8 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, int bj, int h
 // slower when the one before them and its merge still hold part of the SMs, so that
 // their CTAs crowd on the others:
 // - decode_simt_kernel, of which an SM holds several CTAs: the next kernel starts when the
-//   merge runs (called back to back, bf16, 16 heads, 8 sequences of 3000: 303 us by itself
-//   and up to 429 with 3 splits, 194 and 302 with 5);
+//   merge runs (called back to back, bf16, 16 heads, 8 sequences of 3000: 2 splits 503 us
+//   for 443, 3 splits 303 for 298, 5 splits 291 for 189);
 // - the E4M3 pair kernel, with 3 to 8 splits that leave a third of the SMs free: the next
 //   kernel starts when the merge is done (back to back, 8 sequences of 8000: 3 splits 106
 //   to 113 us for 89, 4 splits 91 to 98 for 75, 12 sequences and 3 splits 125 for 104; with

@@ -17,7 +17,7 @@
 // second kernel does with as many CTAs as there is table.
 //
 // Measured (device, with the 1 to 2 us copy that restores the state before each
-// call): 64 sequences grown 7.0 us, 192 forked 9.9, pages of 64 windows given back
+// call): 64 sequences grown 7.3 us, 192 forked 9.7, pages of 64 windows given back
 // 4.4, a pool of 2,048 pages compacted 6.5, one of 65,536 10.6. The forks and the
 // large compaction took 18.5 and 15 with three launches, 11.3 and 11.5 with the
 // requests checked before the count and every load awaited by itself.
